@@ -1169,7 +1169,10 @@ cudaError_t launch_tgemm(const slim_layer& L, const uint16_t* X, int M, int tt, 
   // Largest split of K (cluster size, any of 1..8) that keeps >= 4 K steps
   // per CTA and lets every cluster of the grid be resident at once: a cluster
   // left for a second wave doubles the kernel's time.
-  const int smem = tg_smem(std::min(p.cwmax, L.rl16));
+  // The last columns' CTAs lay out their own stage count: 192 columns in five
+  // stages take more than 256 in four, so shared memory is the larger of the two.
+  const int last = L.rl16 - (ceil_div(L.rl16, p.cwmax) - 1) * p.cwmax;
+  const int smem = std::max(tg_smem(std::min(p.cwmax, L.rl16)), tg_smem(last));
   {
     cudaError_t e = ensure_func_attrs(reinterpret_cast<const void*>(k_tgemm), (size_t)smem);
     if (e != cudaSuccess) return e;
