@@ -106,7 +106,12 @@ int device_cc_major() {
   return major;
 }
 
-void set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<int>(e); }
+// The runtime keeps a failed call's error until it is read: read it here, so
+// that the next call's launch checks do not find it.
+void set_last_cuda_error(cudaError_t e) {
+  (void)cudaGetLastError();
+  g_last_cuda_error = static_cast<int>(e);
+}
 
 int last_cuda_error() { return g_last_cuda_error; }
 
