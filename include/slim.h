@@ -368,6 +368,12 @@ slim_status slim_w4_linear(const slim_w4_layer* layer, const uint16_t* X, int M,
                            size_t ws_bytes, void* stream);
 /* Host-only.  Kernels one slim_w4_linear call launches (-1 on a bad argument). */
 int slim_w4_launches(const slim_w4_layer* layer, int M);
+/* Host-only test aid: how the kernel for few tokens splits a call of M tokens:
+ * plan[0] ranks of a cluster along K (rank i owns the 128-column chunks
+ * [i C / ranks, (i + 1) C / ranks) of C = K / 128), plan[1] panels a rank takes
+ * its chunks in, plan[2] chunks of a panel (the last one may hold fewer), plan[3]
+ * CTAs along the rows.  All 0 when a call of M tokens does not run it. */
+slim_status slim_w4_plan(const slim_w4_layer* layer, int M, int32_t plan[4]);
 /* Test aid: q int8 [N][K] and fp16 scales [N][K/group] (device). */
 slim_status slim_w4_unpack(const slim_w4_layer* layer, int8_t* q, uint16_t* scales, void* stream);
 /* Host-only, synchronizing: as slim_sync_status. */

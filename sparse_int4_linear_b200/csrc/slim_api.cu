@@ -474,6 +474,13 @@ slim_status slim_w4_linear(const slim_w4_layer* layer, const uint16_t* X, int M,
   return SLIM_OK;
 }
 
+slim_status slim_w4_plan(const slim_w4_layer* layer, int M, int32_t plan[4]) {
+  if (!w4_ok(layer)) return SLIM_ERR_STATE;
+  if (M < 0 || !plan) return SLIM_ERR_ARG;
+  slim::w4_split(*layer, M, plan);
+  return SLIM_OK;
+}
+
 slim_status slim_w4_unpack(const slim_w4_layer* layer, int8_t* q, uint16_t* scales, void* stream) {
   if (!w4_ok(layer)) return SLIM_ERR_STATE;
   if (!q || !scales) return SLIM_ERR_ARG;

@@ -174,6 +174,7 @@ cudaError_t launch_backward(const slim_layer& L, const uint16_t* X, const uint16
 size_t w4_dec_bytes(int K, int N, int group);
 size_t w4_workspace_bytes(const slim_w4_layer& L, int M);
 int w4_launches(const slim_w4_layer& L, int M);
+void w4_split(const slim_w4_layer& L, int M, int32_t* plan);   // see slim_w4_plan
 cudaError_t launch_w4_pack(const slim_w4_layer& L, const uint16_t* W, cudaStream_t s);
 cudaError_t launch_w4_unpack(const slim_w4_layer& L, int8_t* q, uint16_t* scales, cudaStream_t s);
 cudaError_t launch_w4(const slim_w4_layer& L, const uint16_t* X, int M, uint16_t* Y, void* ws, cudaStream_t s);

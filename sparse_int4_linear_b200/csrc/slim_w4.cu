@@ -514,7 +514,8 @@ W4Plan w4_plan_uncached(const slim_w4_layer& L, int M) {
     // Few panels; rings of 3 stages, or 2, before more panels.
     for (pl.P = 1; pl.P <= nck && pl.smem == 0; ++pl.P) {
       pl.ckp = ceil_div(nck, pl.P);
-      if (ceil_div(nck, pl.ckp) != pl.P) continue;
+      // (The shorter ranks, of NCK / S chunks, have one of the last panel too.)
+      if (ceil_div(nck, pl.ckp) != pl.P || (pl.P - 1) * pl.ckp >= NCK / S) continue;
       // Row tiles of a CTA: an even share of the SMs, but no more than 32 (the
       // segments and sums kept in shared memory).
       const bool keep = S > 1 || pl.P > 1;
@@ -554,6 +555,14 @@ size_t w4_dec_bytes(int K, int N, int group) {
 }
 
 bool w4_streams(const slim_w4_layer& L, int M) { return w4_few(L, M) && w4_plan(L, M).smem > 0; }
+
+void w4_split(const slim_w4_layer& L, int M, int32_t* plan) {
+  const W4Plan pl = M > 0 && w4_streams(L, M) ? w4_plan(L, M) : W4Plan{0, 0, 0, 0, 0, 0, 0, 0};
+  plan[0] = pl.S;
+  plan[1] = pl.P;
+  plan[2] = pl.ckp;
+  plan[3] = pl.G;
+}
 
 size_t w4_workspace_bytes(const slim_w4_layer& L, int M) {
   if (M <= 0 || w4_streams(L, M) || qgemm_pays(M, L.N)) return 0;

@@ -96,6 +96,7 @@ _SIGS = {
     "slim_w4_workspace_bytes": (c_size_t, [_W4, c_int]),
     "slim_w4_launches": (c_int, [_W4, c_int]),
     "slim_w4_linear": (c_int, [_W4, c_void_p, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "slim_w4_plan": (c_int, [_W4, c_int, ctypes.POINTER(ctypes.c_int32)]),
     "slim_w4_unpack": (c_int, [_W4, c_void_p, c_void_p, c_void_p]),
     "slim_w4_sync_status": (c_int, [_W4, c_void_p]),
 }
