@@ -31,7 +31,10 @@ struct NvtxRange {
 //   SLIM_DECODE_CFG     "WR,KW,S" forces the token-tiled decode kernel's split
 //   SLIM_NO_PREFILL     M > 16 stays on the token-tiled decode kernels
 //   SLIM_PREFILL_1SM    the prefill path never uses SM pairs
-//   SLIM_PREFILL_TILE   "halves,tokens" or "pair,tokens" forces a prefill tile
+//   SLIM_PREFILL_TILE   "halves,tokens" or "pair,tokens" forces a prefill tile of the
+//                       forward and the gated block (where that path has it: one half
+//                       64 or 128 tokens in the forward, two 128 or 192, and 64 in the
+//                       gated block; pairs 128, 192, 224 or 240 from 256 tokens on)
 struct Tuning {
   bool no_stream = false, no_prefill = false, prefill_1sm = false, pdl_early = false;
   int stream_warps = 0;                      // 0: chosen per call

@@ -1220,9 +1220,9 @@ PrefillTile prefill_tile(const slim_layer& L, int M) {
   const Tuning tn = tuning();
   bool pair_ok = M >= 256 && !tn.prefill_1sm;
   for (int g = 0; g + 1 < L.n_groups; ++g) pair_ok = pair_ok && L.group_end[g] % 512 == 0;
-  if (tn.prefill_tile) {   // forced tile, for tuning and tests
+  if (tn.prefill_tile) {   // forced tile, for tuning and tests: one that launch_prefill has
     if (tn.prefill_pair && pair_ok) return {tn.prefill_tt, 2, true};
-    if (!tn.prefill_pair) return {tn.prefill_tt, tn.prefill_nh, false};
+    if (!tn.prefill_pair && tn.prefill_tt != (tn.prefill_nh == 1 ? 192 : 64)) return {tn.prefill_tt, tn.prefill_nh, false};
   }
   // Cost of a tile: waves of CTAs x per-CTA time, the latter ~ rows x (TT +
   // 264) (the constant is the per-CTA fixed cost, in token-equivalents,
@@ -1258,6 +1258,12 @@ PrefillTile prefill_tile(const slim_layer& L, int M) {
 // the choice and for the next best pair tile: 256 tokens 88.5 and 85.6, 1024
 // tokens 127 and 126, 2048 tokens 218 and 225.
 PrefillTile gated_tile(const slim_layer& L, int M) {
+  const Tuning tn = tuning();
+  const bool pair_ok = M >= 256 && !tn.prefill_1sm;
+  if (tn.prefill_tile) {   // forced tile
+    if (tn.prefill_pair && pair_ok) return {tn.prefill_tt, 2, true};
+    if (!tn.prefill_pair && tn.prefill_nh == 2) return {tn.prefill_tt, 2, false};
+  }
   const long long nsm = num_sms();
   PrefillTile best = {192, 2, false};
   long long best_cost = -1;
@@ -1269,7 +1275,7 @@ PrefillTile gated_tile(const slim_layer& L, int M) {
       best_cost = cost;
     }
   }
-  if (M >= 256 && !tuning().prefill_1sm)
+  if (pair_ok)
     for (int tt : {240, 224, 192, 128}) {
       const long long ctas = 2LL * (L.N / 512) * ceil_div(M, tt);
       const long long cost = (ctas + nsm - 1) / nsm * (tt + 264);
