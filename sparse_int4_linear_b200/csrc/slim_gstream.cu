@@ -237,7 +237,7 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
   const int pstride = xrows * kGsTok;
 
   bool ok = true;
-  int it = 0, st = 0, gave_up = 0;
+  int it = 0, st = 0, gave_up = 0, gave_pan = 0;   // where a wait gave up: the stage, the panel
   uint32_t ph = 0;
   for (int pan = 0; pan < p.P; ++pan) {
     if (pan > 0) {
@@ -254,6 +254,7 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
     if (ok && !__all_sync(0xffffffffu, mbar_wait(xbar, pan & 1))) {
       ok = false;
       gave_up = it;
+      gave_pan = pan;
     }
     int left = f1 - f0, lt = f0 / p.ckp, c = f0 - lt * p.ckp;
     while (left > 0) {
@@ -261,7 +262,10 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
       for (int q = 0; q < real; q += SC) {
         if (ok) {
           ok = __all_sync(0xffffffffu, mbar_wait_s(bar_s + st * 8, ph));
-          if (!ok) gave_up = it;
+          if (!ok) {
+            gave_up = it;
+            gave_pan = pan;
+          }
         }
         if (ok) {
           const uint32_t wl = wl0 + (uint32_t)(st * SLOT), sl = sl0 + (uint32_t)(st * SLOT);
@@ -304,9 +308,10 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
   }
   if (!ok && lane == 0) {
     record_status(p.status, SLIM_ERR_TIMEOUT);
-    // Let the copies issued and not consumed land before the CTA exits.
+    // Let the copies issued and not consumed land before the CTA exits (X's
+    // last one is that of the panel where warp 0, which issues them, stopped).
     const long long deadline = clock64() + kWaitBudgetCycles;
-    if (warp == 0) drain_phase(xbar, (p.P - 1) & 1, deadline);
+    if (warp == 0) drain_phase(xbar, gave_pan & 1, deadline);
     for (int i = gave_up; i < i_n; ++i) drain_phase(bars + i % nst, (i / nst) & 1, deadline);
   }
   // T = X L of the kernel before this one, and with it everything older.

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const W4Params p) {
   const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(bars);
   const uint32_t wl0 = ring_s + lane * 16, sl0 = ring_s + 1024 + g * 4 * NG;
   bool ok = true;
-  int it = 0, st = 0, gave_up = 0;
+  int it = 0, st = 0, gave_up = 0, gave_pan = 0;   // where a wait gave up: the stage, the panel
   uint32_t ph = 0;
   for (int pan = 0; pan < p.P; ++pan) {
     if (pan > 0) {
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const W4Params p) {
     if (ok && !__all_sync(0xffffffffu, mbar_wait(xbar, pan & 1))) {
       ok = false;
       gave_up = it;
+      gave_pan = pan;
     }
     const int nc = min(p.ckp, nck - pan * p.ckp);
     const int f0 = start(warp, nc);
@@ -387,7 +388,10 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const W4Params p) {
     while (left > 0) {
       if (ok) {
         ok = __all_sync(0xffffffffu, mbar_wait_s(bar_s + st * 8, ph));
-        if (!ok) gave_up = it;
+        if (!ok) {
+          gave_up = it;
+          gave_pan = pan;
+        }
       }
       const int n = min(min(SC, left), nc - c);
       if (ok) {
@@ -464,9 +468,10 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const W4Params p) {
   }
   if (!ok && lane == 0) {
     record_status(p.status, SLIM_ERR_TIMEOUT);
-    // Let the copies issued and not consumed land before the CTA exits.
+    // Let the copies issued and not consumed land before the CTA exits (X's
+    // last one is that of the panel where warp 0, which issues them, stopped).
     const long long deadline = clock64() + kWaitBudgetCycles;
-    if (warp == 0) drain_phase(xbar, (p.P - 1) & 1, deadline);
+    if (warp == 0) drain_phase(xbar, gave_pan & 1, deadline);
     for (int i = gave_up; i < i_n; ++i) drain_phase(bars + i % nst, (i / nst) & 1, deadline);
   }
   if (S > 1) {
