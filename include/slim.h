@@ -44,8 +44,10 @@
  * of SM clock.  The kernel then records SLIM_ERR_TIMEOUT and never leaves a
  * plausible-looking partial result: the output tiles it owns are written as
  * zeros, and an adapter product X·L it could not finish is written as NaN,
- * so the outputs that use it are NaN.  Treat the whole Y of a call after
- * which slim_sync_status() reports SLIM_ERR_TIMEOUT as invalid.
+ * so the outputs that use it are NaN.  The gated block (H and GU), the
+ * backward passes and the dense 4-bit linear write NaN, not zeros.  Treat every
+ * output of a call after which slim_sync_status() reports SLIM_ERR_TIMEOUT as
+ * invalid.
  *
  * Debug build.  libslim_debug.so (built with -DSLIM_DEBUG) checks the index
  * arithmetic of the kernels' global-memory accesses (chunk, tile, segment,
@@ -402,6 +404,15 @@ slim_status slim_test_wait_timeout(const slim_layer* layer, int wait_us, void* s
  * kernel), SLIM_ERR_WORKSPACE, SLIM_ERR_ALIGN, SLIM_ERR_STATE. */
 slim_status slim_test_stream_timeout(const slim_layer* layer, const uint16_t* X, int M, uint16_t* Y,
                                      void* workspace, size_t ws_bytes, int wait_us, void* stream);
+
+/* Test aid for the gated block's rule: runs slim_gated exactly, except that its
+ * CTAs also wait, for about `wait_us` microseconds of SM clock each, for a
+ * barrier that nothing completes.  Every such wait gives up: H and GU are NaN,
+ * and SLIM_ERR_TIMEOUT is recorded in the layer's status word.  The workspace
+ * is left ready for the next call.  Errors: slim_gated's, SLIM_ERR_ARG for
+ * wait_us < 1, and SLIM_ERR_UNSUPPORTED for more tiles than run at once. */
+slim_status slim_test_gated_timeout(const slim_layer* layer, const uint16_t* X, int M, int act, uint16_t* H,
+                                    uint16_t* GU, void* workspace, size_t ws_bytes, int wait_us, void* stream);
 
 /* Test aid: expand the DECODE stream layout back into dense int8 q [N][K]
  * (zeros at pruned positions) and fp16 scales [N][K/128] (device), so the

@@ -92,6 +92,15 @@ slim_status check_device() {
   return major == 10 ? SLIM_OK : SLIM_ERR_UNSUPPORTED;
 }
 
+// `wait_us` microseconds in SM cycles of the current device, at most the
+// kernels' wait budget.
+cudaError_t wait_cycles(int wait_us, long long* cycles) {
+  int khz = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, slim::current_device());
+  *cycles = std::min<long long>((long long)wait_us * khz / 1000, slim::kWaitBudgetCycles);
+  return e;
+}
+
 // The device ranges [a, a + an) and [b, b + bn) share a byte.
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -360,9 +369,8 @@ int slim_gated_launches(const slim_layer* layer, int M) {
   return slim::gated_launches(*layer, M);
 }
 
-slim_status slim_gated(const slim_layer* layer, const uint16_t* X, int M, int act, uint16_t* H, uint16_t* GU,
-                       void* workspace, size_t ws_bytes, void* stream) {
-  slim::NvtxRange nv("slim_gated");
+static slim_status gated(const slim_layer* layer, const uint16_t* X, int M, int act, uint16_t* H, uint16_t* GU,
+                         void* workspace, size_t ws_bytes, void* stream, int fail_us) {
   if (!layer_ok(layer)) return SLIM_ERR_STATE;
   if (M < 0 || !act_ok(act)) return SLIM_ERR_ARG;
   if (!gated_ok(layer)) return SLIM_ERR_SHAPE;
@@ -376,9 +384,28 @@ slim_status slim_gated(const slim_layer* layer, const uint16_t* X, int M, int ac
     return SLIM_ERR_ARG;
   slim_status st = check_device();
   if (st != SLIM_OK) return st;
-  cudaError_t e = slim::launch_gated(*layer, X, M, act, H, GU, workspace, static_cast<cudaStream_t>(stream));
+  long long fail_cycles = 0;
+  cudaError_t e = cudaSuccess;
+  if (fail_us > 0) {
+    e = wait_cycles(fail_us, &fail_cycles);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  e = slim::launch_gated(*layer, X, M, act, H, GU, workspace, static_cast<cudaStream_t>(stream), fail_cycles);
+  if (fail_us > 0 && e == cudaErrorNotSupported) return SLIM_ERR_UNSUPPORTED;
   if (e != cudaSuccess) return cuda_fail(e);
   return SLIM_OK;
+}
+
+slim_status slim_gated(const slim_layer* layer, const uint16_t* X, int M, int act, uint16_t* H, uint16_t* GU,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  slim::NvtxRange nv("slim_gated");
+  return gated(layer, X, M, act, H, GU, workspace, ws_bytes, stream, 0);
+}
+
+slim_status slim_test_gated_timeout(const slim_layer* layer, const uint16_t* X, int M, int act, uint16_t* H,
+                                    uint16_t* GU, void* workspace, size_t ws_bytes, int wait_us, void* stream) {
+  if (wait_us < 1) return layer_ok(layer) ? SLIM_ERR_ARG : SLIM_ERR_STATE;
+  return gated(layer, X, M, act, H, GU, workspace, ws_bytes, stream, wait_us);
 }
 
 size_t slim_backward_workspace_bytes(const slim_layer* layer, int M) {
@@ -517,10 +544,9 @@ slim_status slim_test_stream_timeout(const slim_layer* layer, const uint16_t* X,
   if (!slim::stream_supported(*layer, M)) return SLIM_ERR_UNSUPPORTED;
   const size_t need = slim::stream_workspace_bytes(*layer, M);
   if (!workspace || ws_bytes < need) return SLIM_ERR_WORKSPACE;
-  int dev = slim::current_device(), khz = 0;
-  cudaError_t e = cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, dev);
+  long long cycles = 0;
+  cudaError_t e = wait_cycles(wait_us, &cycles);
   if (e != cudaSuccess) return cuda_fail(e);
-  const long long cycles = std::min<long long>((long long)wait_us * khz / 1000, slim::kWaitBudgetCycles);
   e = slim::launch_stream_ex(*layer, X, M, Y, workspace, cycles, 1u, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   return SLIM_OK;

@@ -833,13 +833,14 @@ int gated_launches(const slim_layer& L, int M) {
 }
 
 cudaError_t launch_gated(const slim_layer& L, const uint16_t* X, int M, int act, uint16_t* H, uint16_t* GU, void* ws,
-                         cudaStream_t s) {
+                         cudaStream_t s, long long fail_cycles) {
   if (M <= 0) return cudaSuccess;
   GatedOut o;
   o.Y = H;
   o.gated = true;
   o.act = act;
   o.GU = GU;
+  o.fail_cycles = fail_cycles;
   uint8_t* wb = static_cast<uint8_t*>(ws) + 1024;
   uint16_t* T = L.r16 > 0 ? reinterpret_cast<uint16_t*>(wb) : nullptr;
   cudaError_t e = cudaSuccess;

@@ -51,6 +51,7 @@ struct GsParams {
   int P, ckp;          // panels of K, chunks of a panel (the last one may lack some)
   int tmax;            // row tiles of the largest CTA
   int act;
+  long long fail_cycles;   // test aid (see GatedOut)
   int32_t* status;
 };
 
@@ -61,7 +62,7 @@ __host__ __device__ inline GsSmem gs_smem(int slot, int xrows, int ckp, int nst,
   GsSmem m;
   size_t off = 0;
   m.ring = off; off += (size_t)kGsWarps * nst * slot;
-  m.bars = off; off += (size_t)(kGsWarps * kGsStages + 2) * 8;        // the rings', X's
+  m.bars = off; off += (size_t)(kGsWarps * kGsStages + 2) * 8;        // the rings', X's, one that never completes
   m.who = off;  off += (size_t)(tmax * 8 + 15) / 16 * 16;             // first and last warp of a tile
   m.part = off; off += (size_t)(tmax + kGsWarps) * xrows * kGsTok * 4;
   m.ts = off;   off += rl16 > 0 ? (size_t)xrows * (rl16 + 8) * 2 : 0;
@@ -196,7 +197,10 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
   };
   if (lane == 0) {
     for (int i = 0; i < nst; ++i) mbar_init(bars + i, 1);
-    if (warp == 0) mbar_init(xbar, 1);
+    if (warp == 0) {
+      mbar_init(xbar, 1);
+      mbar_init(xbar + 1, 1);
+    }
     fence_mbar_init();
   }
   __syncwarp();
@@ -236,7 +240,7 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
   const uint32_t wl0 = ring_s + lane * 16, sl0 = ring_s + 1536 + 8 * g;
   const int pstride = xrows * kGsTok;
 
-  bool ok = true;
+  bool ok = p.fail_cycles == 0 || __all_sync(0xffffffffu, mbar_wait(xbar + 1, 0, p.fail_cycles));
   int it = 0, st = 0, gave_up = 0, gave_pan = 0;   // where a wait gave up: the stage, the panel
   uint32_t ph = 0;
   for (int pan = 0; pan < p.P; ++pan) {
@@ -324,7 +328,7 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
           __ldcg(reinterpret_cast<const uint4*>(p.T + (size_t)(tok0 + tk) * p.rl16 + c8));
     }
   }
-  // A CTA one of whose waits gave up stores zeros.
+  // A CTA one of whose waits gave up stores NaN.
   const bool bad = __syncthreads_or(!ok);
   const int F = p.N >> 1, JS = p.r16 / 16;
   const uint32_t ts_s = smem_u32(Ts);
@@ -382,7 +386,7 @@ __global__ void __maxnreg__(112) k_gstream(const GsParams p) {
       for (int i = 0; i < 4; ++i) {
         const int tk = n * 8 + 2 * t + (i & 1), row = n0 + 8 * (i >> 1);
         if (tk >= xrows || !dcheck(row < F && tok0 + tk < p.M, p.status)) continue;
-        const float gv = bad ? 0.f : y[0][n][i], uv = bad ? 0.f : y[1][n][i];
+        const float gv = bad ? NAN : y[0][n][i], uv = bad ? NAN : y[1][n][i];
         p.H[(size_t)(tok0 + tk) * F + row] = __bfloat16_as_ushort(__float2bfloat16_rn(act_fwd(p.act, gv) * uv));
         if (p.GU) {
           p.GU[(size_t)(tok0 + tk) * p.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(gv));
@@ -481,6 +485,7 @@ cudaError_t launch_gstream(const slim_layer& L, const uint16_t* X, int M, const 
   p.ckp = pl.ckp;
   p.tmax = pl.tmax;
   p.act = o.act;
+  p.fail_cycles = o.fail_cycles;
   p.status = L.status;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.G, ceil_div(M, 16));

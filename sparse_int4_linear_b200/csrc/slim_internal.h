@@ -96,6 +96,9 @@ struct GatedOut {
   bool gated = false;
   int act = 0;
   uint16_t* GU = nullptr;
+  // Test aid: the gated kernels also wait that many SM cycles for something
+  // that never comes (0: they do not), and so give up.
+  long long fail_cycles = 0;
 };
 
 // Adapter down-projection T = X L into `T` (bf16 [ceil(M/16)*16][r16]).
@@ -164,7 +167,7 @@ cudaError_t launch_prefill(const slim_layer& L, const uint16_t* X, int M, const 
 size_t gated_workspace_bytes(const slim_layer& L, int M);
 int gated_launches(const slim_layer& L, int M);
 cudaError_t launch_gated(const slim_layer& L, const uint16_t* X, int M, int act, uint16_t* H, uint16_t* GU, void* ws,
-                         cudaStream_t s);
+                         cudaStream_t s, long long fail_cycles = 0);
 
 // Backward pass of the linears (dY) or, with dY null, of the gated block (GU,
 // dH, act); null outputs are not computed.

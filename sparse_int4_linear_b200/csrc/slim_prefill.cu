@@ -97,6 +97,7 @@ struct PrefillParams {
   // H [M][F], and GU [M][2F], when not null, receives G and U.
   uint16_t* GU;
   int act;
+  long long fail_cycles;                // test aid (see GatedOut)
 };
 
 // Named barrier 1 of the 256 epilogue threads that also returns the OR of
@@ -115,7 +116,9 @@ __device__ __forceinline__ bool epi_bar_or(bool v) {
 // (columns 0 .. TT of tensor memory) and the matching 128 up rows (TT ..
 // 2 TT), so lane L of a warp's quarter holds G and U of the same row.  The two
 // warp groups take the 32-token chunks in turn; H (and G, U) go through shared
-// memory to whole-line stores.  n0: the CTA's first row of H.
+// memory to whole-line stores.  n0: the CTA's first row of H.  Where a wait gave
+// up everything is NaN: zeros would pass for a gate that is shut, and as G and U
+// for gradients that vanish.
 template <int TT>
 __device__ __forceinline__ void gated_epilogue(const PrefillParams& p, uint32_t tmem, uint16_t* stage, bool stage_ok,
                                                int n0, int t0) {
@@ -144,18 +147,19 @@ __device__ __forceinline__ void gated_epilogue(const PrefillParams& p, uint32_t 
   const bool bad = epi_bar_or(!stage_ok);
   if (bad && threadIdx.x == 0) record_status(p.status, SLIM_ERR_TIMEOUT);
   const int ntok = min(TT, p.M - t0);
+  const uint4 nan8 = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
   for (int i = threadIdx.x; i < ntok * 16; i += 256) {
     const int tk = i >> 4, c8 = (i & 15) * 8;
     if (!dcheck(t0 + tk < p.M && n0 + c8 + 8 <= F, p.status)) continue;
     *reinterpret_cast<uint4*>(p.Y + (size_t)(t0 + tk) * F + n0 + c8) =
-        bad ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(stage + tk * TILE_ROWS + c8);
+        bad ? nan8 : *reinterpret_cast<const uint4*>(stage + tk * TILE_ROWS + c8);
   }
   if (!p.GU) return;
   for (int i = threadIdx.x; i < ntok * 32; i += 256) {
     const int tk = i >> 5, c8 = (i & 31) * 8;
     if (!dcheck(t0 + tk < p.M, p.status)) continue;
     *reinterpret_cast<uint4*>(p.GU + (size_t)(t0 + tk) * p.N + (c8 < TILE_ROWS ? n0 + c8 : F + n0 + c8 - TILE_ROWS)) =
-        bad ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(gs + tk * 256 + c8);
+        bad ? nan8 : *reinterpret_cast<const uint4*>(gs + tk * 256 + c8);
   }
 }
 
@@ -430,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefill(const __grid_constant__
     // Warp-uniform: the tensor-memory loads below are .sync.aligned.
     const bool stage_ok = __all_sync(0xffffffffu, acc_ok && !*abort_flag);
     if constexpr (GATED) {
-      gated_epilogue<TT>(p, tmem, stage, stage_ok, rp * TILE_ROWS, t0);
+      // (A second completion of acc_full never comes.)
+      const bool shown = stage_ok && (p.fail_cycles == 0 || __all_sync(0xffffffffu, mbar_wait(acc_full, 1, p.fail_cycles)));
+      gated_epilogue<TT>(p, tmem, stage, shown, rp * TILE_ROWS, t0);
     } else {
       if (stage_ok && h < NH) {
         const int rloc = h * TILE_ROWS + L;
@@ -809,8 +815,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefill2(const __grid_constant_
       // guarantees that no MMA is in flight when the pair frees tensor memory
       // (rank 1 frees only after the closing cluster barrier).  Rank 1 gets it
       // only for complete accumulators.  Once a wait has given up, this and
-      // all later tiles are stored as zeros.
+      // all later tiles are stored as zeros (GATED: as NaN, see gated_epilogue).
       if (good) good = rank == 0 ? mbar_wait(acc_full, n & 1) : pwait(acc_full, n & 1, abort_flag);
+      // (The next completion of acc_full never comes while a pair has one tile.)
+      if (GATED && good && p.fail_cycles) good = mbar_wait(acc_full, (n & 1) ^ 1, p.fail_cycles);
       good = __all_sync(0xffffffffu, good && !*abort_flag);
       tc_fence_after();
       if (!good) *abort_flag = 1;
@@ -835,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefill2(const __grid_constant_
           float gf[2][16], uf[2][16];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            gf[c >> 4][c & 15] = good ? __uint_as_float(gr[c >> 4][c & 15]) : 0.f;
-            uf[c >> 4][c & 15] = good ? __uint_as_float(ur[c >> 4][c & 15]) : 0.f;
+            gf[c >> 4][c & 15] = good ? __uint_as_float(gr[c >> 4][c & 15]) : NAN;
+            uf[c >> 4][c & 15] = good ? __uint_as_float(ur[c >> 4][c & 15]) : NAN;
           }
           if (p.GU) {
             uint16_t* gu = p.GU + (size_t)(t0 + c0) * p.N + n0;
@@ -1318,6 +1326,7 @@ cudaError_t launch_prefill_tt(const slim_layer& L, const uint16_t* X, int M, con
   p.Y = o.Y;
   p.GU = o.GU;
   p.act = o.act;
+  p.fail_cycles = o.fail_cycles;
   p.M = M;
   p.N = L.N;
   p.K = L.K;
@@ -1389,6 +1398,7 @@ cudaError_t launch_prefill2_tt(const slim_layer& L, const uint16_t* X, int M, co
   p.Y = o.Y;
   p.GU = o.GU;
   p.act = o.act;
+  p.fail_cycles = o.fail_cycles;
   p.M = M;
   p.N = L.N;
   p.K = L.K;
@@ -1416,7 +1426,9 @@ cudaError_t launch_prefill2_tt(const slim_layer& L, const uint16_t* X, int M, co
   // As many pairs as run at once, or one per tile when there are fewer tiles.
   cfg.gridDim = dim3(2);
   const int pairs = max_clusters(reinterpret_cast<const void*>(k_prefill2<TT, GATED>), cfg);
-  cfg.gridDim = dim3(2 * std::max(1, std::min(pairs, ceil_div(M, TT) * ceil_div(L.N, 512))));
+  const int tiles = ceil_div(M, TT) * ceil_div(L.N, 512);
+  if (o.fail_cycles && tiles > pairs) return cudaErrorNotSupported;   // (its wait needs one tile a pair)
+  cfg.gridDim = dim3(2 * std::max(1, std::min(pairs, tiles)));
   return cudaLaunchKernelEx(&cfg, k_prefill2<TT, GATED>, tmap, tmap_img, tmap_rp, tmap_t, p);
 }
 

@@ -85,6 +85,8 @@ _SIGS = {
     "slim_gated_workspace_bytes": (c_size_t, [_P, c_int]),
     "slim_gated_launches": (c_int, [_P, c_int]),
     "slim_gated": (c_int, [_P, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "slim_test_gated_timeout": (c_int, [_P, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_int,
+                                        c_void_p]),
     "slim_backward_workspace_bytes": (c_size_t, [_P, c_int]),
     "slim_linear_backward": (c_int, [_P, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                      c_void_p]),
