@@ -293,6 +293,8 @@ __global__ void __launch_bounds__(QG_THREADS, 1)
       } else {
 #pragma unroll
         for (int q = 0; q < 32; ++q) v[q] = 0x7FC00000u;   // incomplete sums are stored as NaN
+        // (What goes by way of the rings may meet a copy that lands late, so NaN
+        // is chosen again where it is stored.)
       }
       if (SP > 1) {
         // This rank's sums, rows padded by 4 floats; the rings are idle (every
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1)
           uint16_t* to = p.C + (size_t)(i - lane) * p.ldc + j0 + c0 + lane;
           const int n = min(32, p.I - (i - lane));
 #pragma unroll 8
-          for (int r = 0; r < n; ++r, to += p.ldc) *to = from[r * 34];
+          for (int r = 0; r < n; ++r, to += p.ldc) *to = good ? from[r * 34] : (uint16_t)0x7FC0;
         }
         __syncwarp();
       }
@@ -403,11 +405,13 @@ __global__ void __launch_bounds__(QG_THREADS, 1)
   }
   if (SP > 1) {
     // Rank r adds rows [rows r / SP, rows (r + 1) / SP) over the ranks, in rank
-    // order (a rank that gave up left NaN).
+    // order; NaN if a wait of any rank gave up.
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     tc_fence_before();
     cluster.sync();
+    bool bad = false;
+    for (int q = 0; q < SP; ++q) bad = bad || *cluster.map_shared_rank(const_cast<int*>(abort_flag), q) != 0;
     const int rows = min(QG_ROWS, p.I - i0), r0 = split * rows / SP, r1 = (split + 1) * rows / SP;
     // (A warp reads whole lines of a rank at a time.)
     for (int e = threadIdx.x; e < (r1 - r0) * (QG_COLS / 4); e += QG_THREADS) {
@@ -424,6 +428,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1)
         if (q < SP) {
           f[0] += v[q].x; f[1] += v[q].y; f[2] += v[q].z; f[3] += v[q].w;
         }
+      if (bad) f[0] = f[1] = f[2] = f[3] = NAN;
       uint16_t* out = p.C + (size_t)(i0 + row) * p.ldc + j0 + j;
       if (j0 + j + 4 <= p.J && (p.ldc & 3) == 0) {
         *reinterpret_cast<uint2*>(out) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
