@@ -365,6 +365,14 @@ def _addr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _scratch(ws: torch.Tensor, layer) -> tuple[int, int]:
+    """Address and bytes of a workspace, which lies in one piece on the layer's
+    device (the library takes the caller's word for both)."""
+    if ws.get_device() != layer.device_index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {layer.device}, where the layer is, got one on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _tokens(t: torch.Tensor, width: int, layer, name: str):
     """(M, t) for a bf16 tensor [M][width] on the layer's device, made contiguous."""
     shape = t.shape
@@ -416,7 +424,7 @@ def gated(layer: PackedLayer, X: torch.Tensor, act: str = "silu", keep: bool = F
         GU = _output(GU, (M, layer.N), layer, "GU")
     if ws is None:
         ws = gated_workspace(layer, M)
-    rc = _gated(layer.ref, X.data_ptr(), M, a, H.data_ptr(), _addr(GU), ws.data_ptr(), ws.numel(),
+    rc = _gated(layer.ref, X.data_ptr(), M, a, H.data_ptr(), _addr(GU), *_scratch(ws, layer),
                 _raw_stream(layer.device_index))
     if rc:
         _check(rc, "slim_gated")
@@ -456,7 +464,7 @@ def linear_backward(layer: PackedLayer, X: torch.Tensor | None, dY: torch.Tensor
     if ws is None:
         ws = backward_workspace(layer, M)
     _check(_lib.slim_linear_backward(layer.ref, _addr(X), dY.data_ptr(), M, _addr(dX), _addr(dL), _addr(dR),
-                                     ws.data_ptr(), ws.numel(), _raw_stream(layer.device_index)),
+                                     *_scratch(ws, layer), _raw_stream(layer.device_index)),
            "slim_linear_backward")
     return dX, dL, dR
 
@@ -479,7 +487,7 @@ def gated_backward(layer: PackedLayer, X: torch.Tensor | None, GU: torch.Tensor,
     if ws is None:
         ws = backward_workspace(layer, M)
     _check(_lib.slim_gated_backward(layer.ref, _addr(X), GU.data_ptr(), dH.data_ptr(), M, a, _addr(dX), _addr(dL),
-                                    _addr(dR), ws.data_ptr(), ws.numel(), _raw_stream(layer.device_index)),
+                                    _addr(dR), *_scratch(ws, layer), _raw_stream(layer.device_index)),
            "slim_gated_backward")
     return dX, dL, dR
 
@@ -552,7 +560,7 @@ def w4_linear(layer: W4Layer, X: torch.Tensor, Y: torch.Tensor | None = None, ws
             ws = w4_workspace(layer, M)
             rc = _w4_linear(layer.ref, X.data_ptr(), M, Y.data_ptr(), ws.data_ptr(), ws.numel(), s)
     else:
-        rc = _w4_linear(layer.ref, X.data_ptr(), M, Y.data_ptr(), ws.data_ptr(), ws.numel(), s)
+        rc = _w4_linear(layer.ref, X.data_ptr(), M, Y.data_ptr(), *_scratch(ws, layer), s)
     _check(rc, "slim_w4_linear")
     return Y
 
