@@ -461,6 +461,8 @@ def linear_backward(layer: PackedLayer, X: torch.Tensor | None, dY: torch.Tensor
     if X is not None:
         X = _input(X, (M, layer.K), layer, "X")
     dX, dL, dR = _gradients(layer, M, need, dX, dL, dR)
+    if dX is dL is dR is None and need:
+        return None, None, None     # only gradients of an adapter that the layer lacks
     if ws is None:
         ws = backward_workspace(layer, M)
     _check(_lib.slim_linear_backward(layer.ref, _addr(X), dY.data_ptr(), M, _addr(dX), _addr(dL), _addr(dR),
@@ -484,6 +486,8 @@ def gated_backward(layer: PackedLayer, X: torch.Tensor | None, GU: torch.Tensor,
     if X is not None:
         X = _input(X, (M, layer.K), layer, "X")
     dX, dL, dR = _gradients(layer, M, need, dX, dL, dR)
+    if dX is dL is dR is None and need:
+        return None, None, None     # only gradients of an adapter that the layer lacks
     if ws is None:
         ws = backward_workspace(layer, M)
     _check(_lib.slim_gated_backward(layer.ref, _addr(X), GU.data_ptr(), dH.data_ptr(), M, a, _addr(dX), _addr(dL),
