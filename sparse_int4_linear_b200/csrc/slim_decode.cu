@@ -32,6 +32,7 @@
 #include <utility>
 
 #include "slim_common.cuh"
+#include "slim_gemm.h"
 #include "slim_internal.h"
 
 namespace cg = cooperative_groups;
@@ -521,11 +522,14 @@ cudaError_t run_decode(DecodeParams p, int S, int n_rg, int n_tt, cudaStream_t s
   return launch_ex(kern, dim3(S, n_rg, n_tt), dim3(WR * KW * 32), smem, S, s, p);
 }
 
+size_t adapter_smem(int NT, int xrow) {
+  return (size_t)NT * 8 * xrow * 2 + 4 * kAdStages * kAdChunkSteps * 512 + 4 * 256 * 4 + (4 * kAdStages + 1) * 8 + 16;
+}
+
 template <int NT>
 cudaError_t run_adapter(const AdParams& p, int S, int n_jg, int n_tt, cudaStream_t s) {
   auto kern = k_adapter_down<NT>;
-  const size_t smem = (size_t)NT * 8 * p.xrow * 2 + 4 * kAdStages * kAdChunkSteps * 512 + 4 * 256 * 4 +
-                      (4 * kAdStages + 1) * 8 + 16;
+  const size_t smem = adapter_smem(NT, p.xrow);
   cudaError_t e = prepare(kern, smem, S);
   if (e != cudaSuccess) return e;
   return launch_ex(kern, dim3(S, n_jg, n_tt), dim3(128), smem, S, s, p);
@@ -618,6 +622,27 @@ cudaError_t launch_adapter_down(const slim_layer& L, const uint16_t* X, int M, u
   p.r16 = L.rl16;   // T columns of all fused linears
   p.xrow = ceil_div(KS, S) * 16 + 8;
   p.status = L.status;
+  // Rows of which 16 ranks do not fit their share of X in shared memory (above
+  // 81,152 columns; above 162,304 up to 8 tokens): the tensor-core product over
+  // the same factor's images, which writes the same T.  It too has seen X
+  // complete when the kernel behind it starts.
+  if (adapter_smem(M <= 8 ? 1 : 2, p.xrow) > 227 * 1024) {
+    GemmCall g;
+    g.I = M;
+    g.J = L.rl16;
+    g.a[0].base = X;
+    g.a[0].rows = M;
+    g.a[0].c = g.a[0].pitch = L.K;
+    g.b[0].base = L.Lp;
+    g.b[0].layout = GemmLayout::kImageK;
+    g.b[0].rows = g.b[0].blk_lines = L.rl16;
+    g.b[0].c = L.K;
+    g.b[0].img_lines = (long long)L.K / 64 * L.rl16;
+    g.C = T;
+    g.ldc = L.rl16;
+    g.status = L.status;
+    return launch_gemms(&g, 1, false, s);
+  }
   if (M <= 8) return run_adapter<1>(p, S, n_jg, n_tt, s);
   return run_adapter<2>(p, S, n_jg, n_tt, s);
 }
