@@ -223,8 +223,10 @@ slim_status slim_unpack_adapters(const slim_layer* layer, int8_t* qL, uint16_t* 
  * the dequantized weight tiles of the tensor-core path (needed with r == 0
  * too).  Zero-fill it once before its first use (for example
  * with cudaMemsetAsync); every call leaves it ready for the next call,
- * whatever layer that call is for.  Calls that may overlap on the GPU need
- * separate workspaces. */
+ * whatever layer that call is for, infinite or NaN inputs included.  The gated
+ * block, the backward passes and the dense 4-bit linear may use the same
+ * workspace (of the largest size any of them needs).  Calls that may overlap on
+ * the GPU need separate workspaces. */
 size_t slim_workspace_bytes(const slim_layer* layer, int M);
 
 /* Forward: Y[M][N] = X[M][K] · W_eff^T + (X · L) · R, bf16 in and out, fp32

@@ -68,7 +68,9 @@ __device__ __forceinline__ void gate_bwd(int block, int blocks, const uint4* __r
 }
 
 // Rows of an odd N moved to a pitch a tensor copy can read (a multiple of 16
-// bytes), 8 columns per thread; the columns past N are never read.
+// bytes), 8 columns per thread; the columns past N are never read.  NaN is made
+// quiet, as arithmetic would: nothing in a workspace may look like the tags of
+// launch_tag().
 __device__ __forceinline__ void pad_rows(int block, int blocks, const uint16_t* __restrict__ src, int N, int P8,
                                          size_t total, uint4* __restrict__ dst) {
   for (size_t e = (size_t)block * 256 + threadIdx.x; e < total; e += (size_t)blocks * 256) {
@@ -77,7 +79,10 @@ __device__ __forceinline__ void pad_rows(int block, int blocks, const uint16_t* 
     const uint16_t* from = src + m * N + c;
     uint32_t o[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) o[q] = c + q < N ? __ldg(from + q) : 0u;
+    for (int q = 0; q < 8; ++q) {
+      o[q] = c + q < N ? __ldg(from + q) : 0u;
+      if ((o[q] & 0x7FFFu) > 0x7F80u) o[q] |= 0x40u;
+    }
     dst[e] = make_uint4(o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16);
   }
 }

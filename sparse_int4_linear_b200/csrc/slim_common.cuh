@@ -243,14 +243,15 @@ __device__ __forceinline__ void st_release_u32(uint32_t* p, uint32_t v) {
 
 // Tag of one launch of the single-launch decode kernel, carried in the high
 // half of the 64-bit words it leaves in a workspace (seq = the workspace's
-// launch count).  Tags lie in [0x7F800001, 0x7FBFFFFE]: read as the high
-// half of a word of fp32 data that is an fp32 NaN, of bf16 or fp16 data a
-// +Inf or a NaN, of tensor-core metadata words an invalid 2:4 position
-// pair.  So no word that any kernel of the library writes from finite data
-// (T tiles, weight images, fp32 partial sums) can look like a current tag,
-// whatever layer or path used the workspace before; consecutive launches
-// differ, and a tag repeats only after 2^22 - 2 launches.
-__host__ __device__ __forceinline__ uint32_t launch_tag(uint32_t seq) { return 0x7F800001u + seq % 0x3FFFFEu; }
+// launch count).  Tags lie in [0x7F810001, 0x7FBFFFFE]: read as the high half
+// of a word of fp32 data, or as a pair of bf16, that is a signalling NaN, which
+// no arithmetic and no conversion produces (their NaN are quiet: 0x7FC0 or
+// 0x7FFF and up; +Inf is 0x7F80), of tensor-core metadata words an invalid 2:4
+// position pair.  So no word that any kernel of the library computes (T and dT,
+// gradients, weight images, fp32 partial sums), infinite or not, can look like a
+// current tag, whatever layer or path used the workspace before; consecutive
+// launches differ, and a tag repeats only after 4,128,766 launches.
+__host__ __device__ __forceinline__ uint32_t launch_tag(uint32_t seq) { return 0x7F810001u + seq % 0x3EFFFEu; }
 
 // 64-bit words read and written as single accesses (a value and its tag
 // arrive together).

@@ -53,7 +53,7 @@
 // sequence number, [1] finished CTAs (rewound to zero by the launch that
 // raised it).  The last CTA to finish advances the sequence number.  Every word
 // this kernel relies on carries the launch's tag (launch_tag(): a bit range
-// that no finite data written by any kernel of the library can produce), so
+// that no data computed by any kernel of the library can have), so
 // whatever another layer or another path left in the workspace is never
 // mistaken for a value of this launch; only words [0] and [1] must be left
 // alone by the other paths, which start their data 256 bytes in.
