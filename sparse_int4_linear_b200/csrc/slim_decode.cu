@@ -503,23 +503,18 @@ cudaError_t prepare(Kern kern, size_t smem, int cluster_x) {
   return ensure_func_attrs(reinterpret_cast<const void*>(kern), smem, cluster_x > 8);
 }
 
+// Row tiles and K-warps of a CTA, ranks of a cluster, ring stages of a warp.
+struct DecodePlan {
+  int WR = 1, KW = 8, S = 1, nst = 0, ad_slots = 0;
+  size_t smem = 0;
+};
+
 template <int NT, int WR, int KW>
-cudaError_t run_decode(DecodeParams p, int S, int n_rg, int n_tt, cudaStream_t s) {
+cudaError_t run_decode(const DecodeParams& p, const DecodePlan& pl, int n_tt, cudaStream_t s) {
   auto kern = k_decode<NT, WR, KW>;
-  // ring depth: all of a warp's K blocks when they fit, else kMaxStages
-  p.nst = std::min(kMaxStages, ceil_div(p.seg_kb_max, KW));
-  p.ad_slots = p.r16 > 0 ? ceil_div(WR, S) : 0;
-  auto bytes = [&]() {
-    return decode_smem(WR, KW, p.seg_kb_max, p.nst, p.ad_slots, p.r16, p.rl16, p.xrows_alloc).total;
-  };
-  size_t smem = bytes();
-  while (smem > 200 * 1024 && p.nst > 2) {
-    --p.nst;
-    smem = bytes();
-  }
-  cudaError_t e = prepare(kern, smem, S);
+  cudaError_t e = prepare(kern, pl.smem, pl.S);
   if (e != cudaSuccess) return e;
-  return launch_ex(kern, dim3(S, n_rg, n_tt), dim3(WR * KW * 32), smem, S, s, p);
+  return launch_ex(kern, dim3(pl.S, ceil_div(p.NRT, WR), n_tt), dim3(WR * KW * 32), pl.smem, pl.S, s, p);
 }
 
 size_t adapter_smem(int NT, int xrow) {
@@ -547,13 +542,68 @@ bool decode_override(int& wr, int& kw, int& s) {
 }
 
 template <int NT>
-cudaError_t dispatch_decode(const DecodeParams& p, int WR, int KW, int S, int n_rg, int n_tt, cudaStream_t s) {
-  if (WR == 1 && KW == 8) return run_decode<NT, 1, 8>(p, S, n_rg, n_tt, s);
-  if (WR == 1 && KW == 4) return run_decode<NT, 1, 4>(p, S, n_rg, n_tt, s);
-  if (WR == 2 && KW == 4) return run_decode<NT, 2, 4>(p, S, n_rg, n_tt, s);
-  if (WR == 4 && KW == 2) return run_decode<NT, 4, 2>(p, S, n_rg, n_tt, s);
-  if (WR == 8 && KW == 1) return run_decode<NT, 8, 1>(p, S, n_rg, n_tt, s);
-  return run_decode<NT, 4, 1>(p, S, n_rg, n_tt, s);
+cudaError_t dispatch_decode(const DecodeParams& p, const DecodePlan& pl, int n_tt, cudaStream_t s) {
+  const int WR = pl.WR, KW = pl.KW;
+  if (WR == 1 && KW == 8) return run_decode<NT, 1, 8>(p, pl, n_tt, s);
+  if (WR == 1 && KW == 4) return run_decode<NT, 1, 4>(p, pl, n_tt, s);
+  if (WR == 2 && KW == 4) return run_decode<NT, 2, 4>(p, pl, n_tt, s);
+  if (WR == 4 && KW == 2) return run_decode<NT, 4, 2>(p, pl, n_tt, s);
+  if (WR == 8 && KW == 1) return run_decode<NT, 8, 1>(p, pl, n_tt, s);
+  return run_decode<NT, 4, 1>(p, pl, n_tt, s);
+}
+
+// The deepest rings (all of a warp's K blocks, or kMaxStages) in 200 KB, at
+// least two stages in what an SM has; false when those do not fit either.
+bool decode_fit(const slim_layer& L, int xrows, DecodePlan& pl) {
+  const int seg = ceil_div(L.n_kblocks, pl.S);
+  pl.ad_slots = L.r16 > 0 ? ceil_div(pl.WR, pl.S) : 0;
+  auto bytes = [&]() { return decode_smem(pl.WR, pl.KW, seg, pl.nst, pl.ad_slots, L.r16, L.rl16, xrows).total; };
+  pl.nst = std::min(kMaxStages, ceil_div(seg, pl.KW));
+  pl.smem = bytes();
+  while (pl.smem > 200 * 1024 && pl.nst > 2) {
+    --pl.nst;
+    pl.smem = bytes();
+  }
+  return pl.smem <= 227 * 1024;
+}
+
+DecodePlan decode_plan(const slim_layer& L, int M) {
+  const int n_tt = ceil_div(M, 16), xrows = std::min(16, M);
+  // Staged X slice budget (bytes): keeps two CTAs per SM.
+  const size_t x_budget = 64 * 1024;
+  DecodePlan pl;
+  if (!decode_override(pl.WR, pl.KW, pl.S)) {
+    const int target = num_sms();
+    if ((size_t)xrows * L.n_kblocks * 512 <= x_budget) {
+      // One row tile per CTA, 8 warps splitting K: no cluster when there are
+      // enough row tiles.
+      while (pl.S < 8 && pl.S < L.n_kblocks && (long long)pl.S * L.n_row_tiles * n_tt < target) pl.S <<= 1;
+    } else {
+      // The X slice must be split along K: 4 row tiles per CTA share it.
+      pl.WR = 4;
+      pl.KW = 1;
+      pl.S = 2;
+      while (pl.S < 16 && pl.S < L.n_kblocks &&
+             ((size_t)xrows * ceil_div(L.n_kblocks, pl.S) * 512 > x_budget ||
+              (long long)pl.S * ceil_div(L.n_row_tiles, pl.WR) * n_tt < 2 * target))
+        pl.S = (pl.S < 8) ? pl.S * 2 : 16;
+    }
+  }
+  pl.S = std::max(1, std::min(pl.S, L.n_kblocks));
+  if (decode_fit(L, xrows, pl)) return pl;
+  // An adapter of thousands of columns (T and R^T tiles in shared memory) or
+  // rows of tens of thousands leave no room: any split that fits, whatever the
+  // number of token tiles.
+  const int shapes[3][2] = {{4, 1}, {1, 8}, {1, 4}};
+  for (const auto& c : shapes)
+    for (int S = 1; S <= std::min(16, L.n_kblocks); ++S) {
+      pl.WR = c[0];
+      pl.KW = c[1];
+      pl.S = S;
+      if (decode_fit(L, xrows, pl)) return pl;
+    }
+  pl.smem = 0;
+  return pl;
 }
 
 }  // namespace
@@ -651,33 +701,8 @@ cudaError_t launch_decode(const slim_layer& L, const uint16_t* X, int M, uint16_
                           cudaStream_t s) {
   NvtxRange nv("decode: sparse product, adapter T R and epilogue (k_decode)");
   const int n_tt = ceil_div(M, 16);
-  const int NT = (M <= 8) ? 1 : 2;
-  const int xrows_alloc = std::min(16, M);
-  // Staged X slice budget (bytes): keeps two CTAs per SM.
-  const size_t x_budget = 64 * 1024;
-  int WR = 1, KW = 8, S = 1;
-  if (!decode_override(WR, KW, S)) {
-    const int target = num_sms();
-    if ((size_t)xrows_alloc * L.n_kblocks * 512 <= x_budget) {
-      // One row tile per CTA, 8 warps splitting K: no cluster when there are
-      // enough row tiles.
-      WR = 1;
-      KW = 8;
-      S = 1;
-      while (S < 8 && S < L.n_kblocks && (long long)S * L.n_row_tiles * n_tt < target) S <<= 1;
-    } else {
-      // The X slice must be split along K: 4 row tiles per CTA share it.
-      WR = 4;
-      KW = 1;
-      S = 2;
-      while (S < 16 && S < L.n_kblocks &&
-             ((size_t)xrows_alloc * ceil_div(L.n_kblocks, S) * 512 > x_budget ||
-              (long long)S * ceil_div(L.n_row_tiles, WR) * n_tt < 2 * target))
-        S = (S < 8) ? S * 2 : 16;
-    }
-  }
-  S = std::max(1, std::min(S, L.n_kblocks));
-  const int n_rg = ceil_div(L.n_row_tiles, WR);
+  const DecodePlan pl = decode_plan(L, M);
+  if (!pl.smem) return cudaErrorNotSupported;
   DecodeParams p;
   p.X = X;
   p.Y = Y;
@@ -693,13 +718,12 @@ cudaError_t launch_decode(const slim_layer& L, const uint16_t* X, int M, uint16_
   p.rl16 = L.rl16;
   p.n_groups = L.n_groups;
   for (int gi = 0; gi < SLIM_MAX_GROUPS; ++gi) p.group_end_rt[gi] = ceil_div(L.group_end[gi], 16);
-  p.seg_kb_max = ceil_div(L.n_kblocks, S);
-  p.nst = 0;
-  p.ad_slots = 0;
-  p.xrows_alloc = xrows_alloc;
+  p.seg_kb_max = ceil_div(L.n_kblocks, pl.S);
+  p.nst = pl.nst;
+  p.ad_slots = pl.ad_slots;
+  p.xrows_alloc = std::min(16, M);
   p.status = L.status;
-  if (NT == 1) return dispatch_decode<1>(p, WR, KW, S, n_rg, n_tt, s);
-  return dispatch_decode<2>(p, WR, KW, S, n_rg, n_tt, s);
+  return M <= 8 ? dispatch_decode<1>(p, pl, n_tt, s) : dispatch_decode<2>(p, pl, n_tt, s);
 }
 
 // (Without an adapter too: the workspace may next serve a layer that has one,
@@ -746,11 +770,15 @@ struct ForwardPlan {
 ForwardPlan forward_plan_uncached(const slim_layer& L, int M, bool allow_prefill, size_t ws_limit) {
   ForwardPlan f;
   if (M <= 0) return f;
-  if (use_prefill(L.rl16, M, allow_prefill)) {
+  const bool stream = use_stream(L, M, ws_limit);
+  // (Where the pair does not fit either, as with an adapter of 4096 columns and
+  // more than 8 tokens, the tensor-core path runs whatever its usual limits.)
+  if (use_prefill(L.rl16, M, allow_prefill) ||
+      (allow_prefill && !tuning().no_prefill && !stream && !decode_plan(L, M).smem)) {
     f.path = Path::kPrefill;
     f.ws = a1k(forward_ctl_bytes(L.r16)) + a1k(t_swz_region(L, M)) + prefill_image_bytes(L.N, L.K);
     f.launches = (L.r16 > 0 ? 1 : 0) + 2;   // [X L] + dequant + main
-  } else if (use_stream(L, M, ws_limit)) {
+  } else if (stream) {
     f.path = Path::kStream;
     f.ws = stream_workspace_bytes(L, M);
     f.launches = 1;
