@@ -284,7 +284,8 @@ typedef enum slim_act { SLIM_ACT_SILU = 0, SLIM_ACT_GELU_TANH = 1 } slim_act;
  * (slim_grouped_layer_init with G = 2 and N_0 = N_1 = F: gate, then up),
  *   H[M][F] = act(G) * U,  G = X Wg^T + (X Lg) Rg,  U = X Wu^T + (X Lu) Ru.
  * bf16 in and out; G, U and the activation are held in fp32 and H is rounded
- * once.  GU may be NULL; otherwise it receives [G, U] as slim_linear would
+ * once.  (4-bit adapters are read as their bf16 images at every token count;
+ * the 4-bit factors are streamed by slim_linear alone.)  GU may be NULL; otherwise it receives [G, U] as slim_linear would
  * write them ([M][2F] bf16), which slim_gated_backward reads.  X, H, GU and
  * the workspace must not overlap.  Workspace (device, >=
  * slim_gated_workspace_bytes(layer, M), zero-filled before its first use):

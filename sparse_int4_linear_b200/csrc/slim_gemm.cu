@@ -15,11 +15,13 @@
 // The pairs are persistent and their sums alternate between two halves of
 // tensor memory, so that the tensor cores work on the next tile while the last
 // one is written (linear backward 11008 x 4096, rank 128, 2048 tokens 198 -> 181
-// us, dense 4-bit 4096 x 11008, 1024 tokens 101 -> 93, 1024 x 20000 70 -> 50).
+// us, dense 4-bit 4096 x 11008, 1024 tokens 101 -> 93, among other calls with cold
+// L2; one after the other they run under the power cap, 213 and 111).
 //
 // Bound by the tensor cores for the large products (a pair's stage is 256 x
 // 256 x 64 MACs = 512 cycles against 32 KB of copies per CTA): dX of 2048
-// tokens, 22016 to 4096, 254 us = 1.45 PFLOP/s on B200.  Bound by latency for
+// tokens, 22016 to 4096, 254 us = 1.45 PFLOP/s on B200.  Of 4096 to 11008 (one
+// launch by itself, cold) the tensor pipe is active for 86 % of an SM's cycles.  Bound by latency for
 // the rank-r ones (a launch, the first copies, a cluster's sums: 5 to 8 us
 // each), which therefore share launches.
 #include <cooperative_groups.h>
@@ -546,9 +548,14 @@ GemmShape gemm_shape(const GemmCall& g) {
 // Columns of a pair's tile when pairs of CTAs, each on 256 rows, fill three
 // quarters of the SMs by themselves, else 0.  256 columns, or for a row-major
 // B the width whose waves of pairs finish first (the constant: a tile's own
-// cost in columns).  Measured, pairs against single CTAs: dX of 11008 x 4096,
-// 2048 tokens 157 us and 170, of 8192 x 8192, 512 tokens 76 and 86; at 64 tiles
-// of pairs, 4096 x 4096, 512 tokens (left to single CTAs), 37.7 and 35.4.
+// cost in columns; 0, 64 and 128 there are within 2 % at 4096 x 11008, 400 and 1024
+// tokens, and 11008 x 4096, 2048).  Measured, pairs against single CTAs, us a call:
+// linear backward 11008 x 4096, rank 128, 2048 tokens 181 and 209, 8192 x 8192, 512
+// tokens 94 and 103, dense 4-bit 4096 x 11008, 1024 tokens 95 and 119, 1024 x 20000
+// 55 and 74.  With 64 CTAs in pairs (left to single CTAs), 4096 x 4096, 512 tokens,
+// 36.0 and 37.2, its backward pass 46.3 and 46.6.  Against it: the backward pass of
+// 8192 x 1024, rank 256, 500 tokens, whose dX has 128 CTAs in pairs of 20 stages
+// each: 45 and 40.
 int pair_width(const GemmShape& h) {
   const int nsm = num_sms();
   const long long rows = (long long)ceil_div(h.I, 256) * h.groups;

@@ -989,9 +989,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1) k_tgemm(const __grid_constant__
         if (!warp_pwait(empty + st, ((it / NST) & 1) ^ 1, abort_flag)) break;
         if (!dcheck(i < p.K / 64, p.status)) break;
         if (one) {
-        mbar_expect_tx(full + st, (uint32_t)(TG_XST + lst));
-        tma_load_2d(xs + st * TG_XST, &tmap_x, i * 64, tile * TG_TOK, full + st);
-        bulk_g2s(ls + st * lst, p.Lp + ((size_t)i * p.rl16 + c0) * 128, (uint32_t)lst, full + st);
+          mbar_expect_tx(full + st, (uint32_t)(TG_XST + lst));
+          tma_load_2d(xs + st * TG_XST, &tmap_x, i * 64, tile * TG_TOK, full + st);
+          bulk_g2s(ls + st * lst, p.Lp + ((size_t)i * p.rl16 + c0) * 128, (uint32_t)lst, full + st);
         }
         ++iss;
       }
@@ -1013,9 +1013,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1) k_tgemm(const __grid_constant__
         tc_fence_after();
         if (one)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_dense(tmem, sw128_desc(xa + st * TG_XST + kk * 32), sw128_desc(la + st * lst + kk * 32), idesc,
-                    (it | kk) != 0);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_dense(tmem, sw128_desc(xa + st * TG_XST + kk * 32), sw128_desc(la + st * lst + kk * 32), idesc,
+                      (it | kk) != 0);
         if (one) tc_commit(empty + st);
       }
       if (one) tc_commit(acc_full);
@@ -1263,8 +1263,9 @@ PrefillTile prefill_tile(const slim_layer& L, int M) {
 // The same choice for the gated block, whose CTAs always hold two accumulators
 // (128 gate rows and the up rows beside them): the two-half tiles, 64 tokens
 // wide for small batches, and the pairs.  4096 to 2 x 11008, us a call for
-// the choice and for the next best pair tile: 256 tokens 88.5 and 85.6, 1024
-// tokens 127 and 126, 2048 tokens 218 and 225.
+// the choice and for the best other tile: 256 tokens 85.2 (one SM, 128) and 83.2
+// (pair, 128), 1024 tokens 125.0 (pair, 224) and 127.4 (pair, 240), 2048 tokens
+// 211.5 (pair, 224) and 218.3 (pair, 240).
 PrefillTile gated_tile(const slim_layer& L, int M) {
   const Tuning tn = tuning();
   const bool pair_ok = M >= 256 && !tn.prefill_1sm;

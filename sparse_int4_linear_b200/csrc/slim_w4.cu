@@ -496,10 +496,13 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) k_w4(const W4Params p) {
 // ---------------------------------------------------------------- host
 constexpr size_t kW4SmemLimit = 220 * 1024;
 // Up to 16 tokens the packed weight is streamed once; up to 32 it is streamed
-// twice where that is shorter than expanding it inside the product: measured
-// (32 tokens) 8192 x 28672 97 us against 111, 4096 x 4096 13.5 against 15.7,
-// 4096 x 11008 29.0 against 26.7, 2048 x 2048 9.6 against 7.9, 1024 x 4096 10.0
-// against 6.1.
+// twice on layers of 2^23 weights or more (which keeps them exact: the product
+// rounds q * s).  Measured, 32 tokens, streamed twice against expanded inside the
+// product, us a call: 8192 x 28672 96.8 and 107.9, 4096 x 4096 13.6 and 15.3, 4096
+// x 2048 10.6 and 12.3; the product would be shorter at 4096 x 11008, 29.0 and
+// 24.8, 11008 x 4096, 34.1 and 29.8, 8192 x 8192, 42.1 and 33.7, 28672 x 8192,
+// 127.6 and 98.9, and is below the limit: 2048 x 2048 9.7 and 8.5, 1024 x 4096 10.1
+// and 6.8.
 bool w4_few(const slim_w4_layer& L, int M) { return M <= 16 || (M <= 32 && (long long)L.N * L.K >= 8 << 20); }
 
 struct W4Plan {
