@@ -256,7 +256,9 @@ slim_status slim_linear(const slim_layer* layer, const uint16_t* X, int M, uint1
 int slim_linear_launches(const slim_layer* layer, int M);
 
 /* Host-only.  Device workspace bytes slim_linear_host needs: the
- * slim_linear workspace plus device staging for X and Y. */
+ * slim_linear workspace plus device staging for X and Y.  (X lies there as it
+ * came: after one that holds signalling NaN, which no arithmetic yields,
+ * zero-fill the workspace before a call of another size or layer.) */
 size_t slim_host_workspace_bytes(const slim_layer* layer, int M);
 
 /* Forward on HOST buffers: copies X_host (M×K bf16, ideally pinned) to the
